@@ -136,8 +136,11 @@ QL_DEV void branch_weight(float (&o)[N], const Args& a, const Mode& k, int c, in
 constexpr int kHeld = 16, kRowVecs = kHeld / kVec;   // values, vectors a thread holds of a row
 
 // work(row, operands) for every row of the workgroup, the operands by
-// load(row, operands): columns past the row's end and rows past the last one
-// stay zero.  AHEAD: the next row is loaded while this one is worked on.
+// load(row, operands): columns past the row's end stay zero.  Side by side with
+// the last rows work is called for rows past the end too, with zeros or an
+// earlier row's operands, so that the barriers are met: nothing of such a row
+// may reach a sum over rows, not even multiplied by zero (its values may not be finite).
+// AHEAD: the next row is loaded while this one is worked on.
 template <bool AHEAD, int RPW, typename Row, typename Load, typename Work>
 QL_DEV void each_row(int64_t m, int sub, Load load, Work work) {
   const int64_t hop = (int64_t)gridDim.x * RPW;
@@ -435,7 +438,6 @@ __global__ __launch_bounds__(kResnormBwdBlock) void k_resnorm_bwd(qlora_resnorm_
     float s2[2] = {0.f, 0.f};   // sums of D p and, with the full gate, g D p
     char* dx = row_of<RT>(a.dx, row, a.lddx);
     char* dgate = FULL ? row_of<AT>(a.dgate, row, a.lddg) : nullptr;
-    const float cg = live ? (FULL ? 1.f : gt) : 0.f;   // a row past the end adds nothing
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       float dg[EV];
@@ -446,14 +448,15 @@ __global__ __launch_bounds__(kResnormBwdBlock) void k_resnorm_bwd(qlora_resnorm_
         const float xy = x * (el(r.y[v], j) * rsy), dp = xy * wb[v][j];
         D[v][j] = x;
         s2[0] += dp;
-        if (live) apre[v][j] += zr * hv;
+        float g = gt;
         if constexpr (FULL) {
-          const float g = el(r.g[v], j);
+          g = el(r.g[v], j);
           s2[1] += dp * g;
-          at[v][j] += xy * (cg * g);
           dg[j] = a.scale * dp;
-        } else {
-          at[v][j] += xy * cg;
+        }
+        if (live) {
+          apre[v][j] += zr * hv;
+          at[v][j] += xy * g;
         }
       }
       if (live && at_col.in[v]) {
