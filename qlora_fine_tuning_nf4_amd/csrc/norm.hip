@@ -19,6 +19,11 @@
 // (with a gate that changes from row to row: T = sum_t g D rms(y), dw_post = s T),
 // so one register array serves both.
 //
+// Sums and products take rows already divided by their root mean square, a
+// value of the size of 1, and the backward factors the root out last: a square
+// or cube of it would leave binary32's range long before the result does (rows of
+// 1e15, or of 1e-14 with eps = 0).
+//
 // Measured: forward of 4096 x 8192 (bf16, fp32 residual) 76 us, 5.3 TB/s;
 // 16384 x 4096 (bf16) 94 us, 5.7 TB/s; one row 3.3 us on the device.  Backward
 // of 16384 x 4096 with all gradients 151 us, 5.3 TB/s (HBM traffic equal to the
@@ -429,7 +434,7 @@ __global__ __launch_bounds__(kResnormBwdBlock) void k_resnorm_bwd(qlora_resnorm_
       }
     row_sum<G>(s3, slots3, slot3);
     const float rsh = k.pre ? __builtin_amdgcn_rsqf(s3[0] * k.inv_d + a.eps) : 0.f;
-    const float ch = rsh * rsh * rsh * s3[1] * k.inv_d;
+    const float ch = s3[1] * rsh * k.inv_d;   // mean(A rms(h))
     const float rsy = k.post ? __builtin_amdgcn_rsqf(s3[2] * k.inv_d + a.eps) : 1.f;
     float gt = 1.f;
     if (k.gate == QLORA_GATE_TOKEN && live) gt = load_param<AT>(a.gate, k.wf32, row);
@@ -443,8 +448,8 @@ __global__ __launch_bounds__(kResnormBwdBlock) void k_resnorm_bwd(qlora_resnorm_
       float dg[EV];
 #pragma unroll
       for (int j = 0; j < EV; ++j) {
-        const float hv = el(r.h[v], j), zr = el(r.dz[v], j) * rsh;
-        const float x = el(r.dh[v], j) + zr * wpre[v][j] - hv * ch;
+        const float hn = el(r.h[v], j) * rsh, z = el(r.dz[v], j);
+        const float x = el(r.dh[v], j) + (z * wpre[v][j] - hn * ch) * rsh;
         const float xy = x * (el(r.y[v], j) * rsy), dp = xy * wb[v][j];
         D[v][j] = x;
         s2[0] += dp;
@@ -455,7 +460,7 @@ __global__ __launch_bounds__(kResnormBwdBlock) void k_resnorm_bwd(qlora_resnorm_
           dg[j] = a.scale * dp;
         }
         if (live) {
-          apre[v][j] += zr * hv;
+          apre[v][j] += z * hn;
           at[v][j] += xy * g;
         }
       }
@@ -470,20 +475,21 @@ __global__ __launch_bounds__(kResnormBwdBlock) void k_resnorm_bwd(qlora_resnorm_
     if (k.gate == QLORA_GATE_TOKEN && a.dgate && live && t == 0)
       gptr_w(reinterpret_cast<float*>(a.dgate))[row] = a.scale * s2[0];
     if (!a.dy || !live) return;
-    // dy = ry q w - y ry^3 mean(q w y), and sum q w y = s / ry sum g D p
-    const float sgt = a.scale * gt * rsy;
-    const float cy = rsy * sgt * s2[FULL] * k.inv_d;
+    // dy = ry s (g D w - rms(y) mean(g D p)), the mean without a post norm left out
+    const float sgt = a.scale * gt * rsy, cy = k.post ? s2[FULL] * k.inv_d : 0.f;
     char* dy = row_of<AT>(a.dy, row, a.lddy);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
 #pragma unroll
       for (int j = 0; j < EV; ++j) {
-        D[v][j] *= sgt * wb[v][j];
+        D[v][j] *= wb[v][j];
         if constexpr (FULL) D[v][j] *= el(r.g[v], j);
       }
       if (k.post)
 #pragma unroll
-        for (int j = 0; j < EV; ++j) D[v][j] -= el(r.y[v], j) * cy;
+        for (int j = 0; j < EV; ++j) D[v][j] -= el(r.y[v], j) * rsy * cy;
+#pragma unroll
+      for (int j = 0; j < EV; ++j) D[v][j] *= sgt;
       if (at_col.in[v]) at_col.template store<AT>(v, dy, D[v]);
     }
   };
@@ -554,7 +560,7 @@ __global__ __launch_bounds__(WT) void k_resnorm_bwd_wide(qlora_resnorm_grad a, f
     }
     row_sum<WT>(s3, slots3, slot3);
     const float rsh = k.pre ? __builtin_amdgcn_rsqf(s3[0] * k.inv_d + a.eps) : 0.f;
-    const float ch = rsh * rsh * rsh * s3[1] * k.inv_d;
+    const float ch = s3[1] * rsh * k.inv_d;   // mean(A rms(h))
     const float rsy = k.post ? __builtin_amdgcn_rsqf(s3[2] * k.inv_d + a.eps) : 1.f;
     float gt = 1.f;
     if (k.gate == QLORA_GATE_TOKEN) gt = load_param<AT>(a.gate, k.wf32, row);
@@ -572,7 +578,7 @@ __global__ __launch_bounds__(WT) void k_resnorm_bwd_wide(qlora_resnorm_grad a, f
         const Raw<AT, EV> dz = loadv<AT, EV>(row_of<AT>(a.dz, row, a.lddz), c, d - c);
         const Raw<RT, EV> h = loadv<RT, EV>(row_of<RT>(a.h, row, a.ldh), c, d - c);
 #pragma unroll
-        for (int j = 0; j < EV; ++j) D[j] += el(dz, j) * rsh * w[j] - el(h, j) * ch;
+        for (int j = 0; j < EV; ++j) D[j] += (el(dz, j) * w[j] - el(h, j) * rsh * ch) * rsh;
       }
     };
     float s2[2] = {0.f, 0.f};
@@ -595,8 +601,8 @@ __global__ __launch_bounds__(WT) void k_resnorm_bwd_wide(qlora_resnorm_grad a, f
       if (k.gate == QLORA_GATE_TOKEN && a.dgate && threadIdx.x == 0)
         gptr_w(reinterpret_cast<float*>(a.dgate))[row] = a.scale * s2[0];
     }
-    const float sgt = a.scale * gt;
-    const float cy = rsy * rsy * sgt * (k.gate == QLORA_GATE_FULL ? s2[1] : s2[0]) * k.inv_d;
+    const float sgt = a.scale * gt * rsy;
+    const float cy = k.post ? (k.gate == QLORA_GATE_FULL ? s2[1] : s2[0]) * k.inv_d : 0.f;
     if (stat) {
       if (threadIdx.x == 0) stat[row] = f32x4_t{rsh, ch, rsy, cy};
       continue;
@@ -615,9 +621,9 @@ __global__ __launch_bounds__(WT) void k_resnorm_bwd_wide(qlora_resnorm_grad a, f
 #pragma unroll
       for (int j = 0; j < EV; ++j) {
         dg[j] = a.scale * D[j] * (el(y, j) * rsy) * w[j];
-        float o = sgt * D[j] * w[j];
-        if (k.gate == QLORA_GATE_FULL) o *= el(g, j);
-        D[j] = k.post ? rsy * o - el(y, j) * cy : o;
+        D[j] *= w[j];
+        if (k.gate == QLORA_GATE_FULL) D[j] *= el(g, j);
+        D[j] = (k.post ? D[j] - el(y, j) * rsy * cy : D[j]) * sgt;
       }
       if (k.gate == QLORA_GATE_FULL && a.dgate) storev<AT, EV, true>(row_of<AT>(a.dgate, row, a.lddg), c, d - c, dg);
       if (a.dy) storev<AT, EV, true>(row_of<AT>(a.dy, row, a.lddy), c, d - c, D);
@@ -653,19 +659,20 @@ __global__ __launch_bounds__(256) void k_resnorm_cols(qlora_resnorm_grad a, cons
     float D[EV], dg[EV];
 #pragma unroll
     for (int j = 0; j < EV; ++j) {
-      const float zr = el(dz, j) * s[0];
-      D[j] = el(dh, j) + zr * wpre[j] - el(h, j) * s[1];
-      sr[j] += zr * el(h, j);
+      const float hn = el(h, j) * s[0];
+      D[j] = el(dh, j) + (el(dz, j) * wpre[j] - hn * s[1]) * s[0];
+      sr[j] += el(dz, j) * hn;
     }
     storev<RT, EV, true>(row_of<RT>(a.dx, r, a.lddx), c, left, D);
     if (!k.branch) continue;
 #pragma unroll
     for (int j = 0; j < EV; ++j) {
-      const float xy = D[j] * (el(y, j) * s[2]), gj = full ? el(g, j) : gt;
-      st[j] += xy * gj;
+      const float yn = el(y, j) * s[2], xy = D[j] * yn;
+      st[j] += xy * (full ? el(g, j) : gt);
       dg[j] = a.scale * xy * wb[j];
-      D[j] *= a.scale * gj * wb[j];
-      if (k.post) D[j] = s[2] * D[j] - el(y, j) * s[3];
+      D[j] *= wb[j];
+      if (full) D[j] *= el(g, j);
+      D[j] = (k.post ? D[j] - yn * s[3] : D[j]) * (a.scale * gt * s[2]);
     }
     if (full && a.dgate) storev<AT, EV, true>(row_of<AT>(a.dgate, r, a.lddg), c, left, dg);
     if (a.dy) storev<AT, EV, true>(row_of<AT>(a.dy, r, a.lddy), c, left, D);

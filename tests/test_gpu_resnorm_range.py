@@ -1,11 +1,12 @@
 """The residual norm over the whole of its accepted range: eps of zero, rows
-side by side with rows past the end.  Oracle and tolerances as in
+side by side with rows past the end, rows of large and small numbers.  Oracle and tolerances as in
 ``test_gpu_resnorm.py``, whose derivation does not depend on eps or on the rows' size."""
 import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_resnorm import _check, _np, _rows
+from oracle import train_ops as T
+from tests.test_gpu_resnorm import _case, _check, _close, _gate_np, _np, _rows
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +48,43 @@ def test_earlier_rows_beside_the_last(q, kind):
         assert torch.equal(dx, dh)
         want = np.sign(_np(y)[row, col]) * np.inf
         assert dw[col].item() == want and torch.isfinite(dw).sum() == d - 1
+
+
+def _sized(q, g, m, d, act, res, kind, sh, sy, eps, offset=0.25):
+    """Both directions with residual rows of the size `sh`, block outputs of the size `sy`, and gradients that keep both
+    terms of dx of one size."""
+    a = _case(g, m, d, act, res, "f32", kind, True, True)
+    a["x"], a["y"] = (_rows(g.standard_normal((m, d)) * s, t) for s, t in ((sh, res), (sy, act)))
+    eps = float(np.float32(eps))
+    kw = dict(scale=0.75, eps=eps, w_offset=offset)
+    args = (_gate_np(a, kind), kind, _np(a["w_post"]), _np(a["w_pre"]), True, True, 0.75, eps, offset)
+    h, z = q.qlora_resnorm_fwd(a["x"], a["y"], a["gate"], a["w_post"], a["w_pre"], **kw)
+    hw, zw = T.resnorm_fwd(_np(a["x"]), _np(a["y"]), *args)
+    mag = np.abs(_np(a["x"])) + np.abs(hw - _np(a["x"]))
+    _close(h, hw, mag, res, name="h")
+    r = 1 / np.sqrt((hw * hw).mean(1, keepdims=True) + eps)
+    w = np.abs(offset + _np(a["w_pre"]))
+    _close(z, zw, r * w * (mag + np.abs(hw) * (r * r * (np.abs(hw) * mag).mean(1, keepdims=True))), act, name="z")
+    h, dz, dh = (_rows(g.standard_normal((m, d)) * s, t) for s, t in ((sh, res), (1.0, act), (1 / sh, res)))
+    for given in (None, dh):
+        got = q.qlora_resnorm_bwd(dz, given, h, a["y"], a["gate"], a["w_post"], a["w_pre"], **kw)
+        want, mg = T.resnorm_bwd(_np(dz), _np(given), _np(h), _np(a["y"]), *args)
+        for k, t in zip(("dx", "dy", "dgate", "dw_post", "dw_pre"), got):
+            if k not in want:
+                continue
+            dt = res if k == "dx" else act if k == "dy" or (k == "dgate" and kind == "full") else "f32"
+            col = k in ("dw_post", "dw_pre") or (k == "dgate" and kind == "channel")
+            _close(t if t.dim() == want[k].ndim else t[:, 0], want[k], mg[k], dt, m * 2.0 ** -24 if col else 0.0, k)
+
+
+@pytest.mark.parametrize("size,eps", [(1e13, 1e-5), (1e15, 1e-5), (1e17, 1e-5), (1e-14, 0.0), (1e-14, 1e-30),
+                                      (1e-17, 0.0)])
+@pytest.mark.parametrize("d", [64, 1001, 4096, 9000])
+def test_large_and_small_rows(q, size, eps, d):
+    """Rows whose squares binary32 holds, though the cube of their root is out of its range."""
+    g = np.random.default_rng(d)
+    for act, res in (("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")):
+        for sh, sy in ((size, size), (size, 1.0), (1.0, size)):
+            _sized(q, g, 3, d, act, res, "channel", sh, sy, eps)
+    for kind in ("none", "token", "full"):
+        _sized(q, g, 3, d, "f32", "f32", kind, size, size, eps)
