@@ -86,6 +86,14 @@ QL_DEV void row_sum(float (&v)[N], float (*slots)[W][N], int& slot) {
   }
 }
 
+// 1 / sqrt(x) to one ulp.  The instruction takes a subnormal x for zero: such an x (rows of
+// 1e-19 and less with eps = 0) is scaled by a power of four first.
+QL_DEV float inv_root(float x) {
+  const bool tiny = x < 0x1p-126f;
+  const float r = __builtin_amdgcn_rsqf(tiny ? x * 0x1p64f : x);
+  return tiny ? r * 0x1p32f : r;
+}
+
 // o *= (or =, SET) w_offset + w for N weights; a missing weight counts as 1.
 template <int AT, bool SET, int N>
 QL_DEV void mul_weight(float (&o)[N], const void* w, bool f32, float offset, int64_t c, int left) {
@@ -269,7 +277,7 @@ __global__ __launch_bounds__(resnorm_fwd_block(G)) void k_resnorm_fwd(qlora_resn
 #pragma unroll
         for (int j = 0; j < EV; ++j) s[0] += el(r.y[v], j) * el(r.y[v], j);
       row_sum<G>(s, slots, slot);
-      sg *= __builtin_amdgcn_rsqf(s[0] * k.inv_d + a.eps);
+      sg *= inv_root(s[0] * k.inv_d + a.eps);
     }
     float h[NV][EV];
     float s[1] = {0.f};
@@ -291,7 +299,7 @@ __global__ __launch_bounds__(resnorm_fwd_block(G)) void k_resnorm_fwd(qlora_resn
     if (!k.pre) return;
     row_sum<G>(s, slots, slot);
     if (!live) return;
-    const float rh = __builtin_amdgcn_rsqf(s[0] * k.inv_d + a.eps);
+    const float rh = inv_root(s[0] * k.inv_d + a.eps);
     char* o = row_of<AT>(a.z, row, a.ldz);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -328,7 +336,7 @@ __global__ __launch_bounds__(WT) void k_resnorm_fwd_wide(qlora_resnorm a) {
         for (int j = 0; j < EV; ++j) s[0] += el(y, j) * el(y, j);
       }
       row_sum<WT>(s, slots, slot);
-      sg *= __builtin_amdgcn_rsqf(s[0] * k.inv_d + a.eps);
+      sg *= inv_root(s[0] * k.inv_d + a.eps);
     }
     auto residual = [&](int c, float (&h)[EV]) {
       const Raw<RT, EV> x = loadv<RT, EV>(row_of<RT>(a.x, row, a.ldx), c, d - c);
@@ -356,7 +364,7 @@ __global__ __launch_bounds__(WT) void k_resnorm_fwd_wide(qlora_resnorm a) {
         for (int j = 0; j < EV; ++j) s[0] += (c + j < d) ? h[j] * h[j] : 0.f;
       }
       row_sum<WT>(s, slots, slot);
-      rh = __builtin_amdgcn_rsqf(s[0] * k.inv_d + a.eps);
+      rh = inv_root(s[0] * k.inv_d + a.eps);
     }
     for (int c = threadIdx.x * EV; c < d; c += WT * EV) {
       float h[EV], w[EV];
@@ -433,9 +441,9 @@ __global__ __launch_bounds__(kResnormBwdBlock) void k_resnorm_bwd(qlora_resnorm_
         s3[2] += yv * yv;
       }
     row_sum<G>(s3, slots3, slot3);
-    const float rsh = k.pre ? __builtin_amdgcn_rsqf(s3[0] * k.inv_d + a.eps) : 0.f;
+    const float rsh = k.pre ? inv_root(s3[0] * k.inv_d + a.eps) : 0.f;
     const float ch = s3[1] * rsh * k.inv_d;   // mean(A rms(h))
-    const float rsy = k.post ? __builtin_amdgcn_rsqf(s3[2] * k.inv_d + a.eps) : 1.f;
+    const float rsy = k.post ? inv_root(s3[2] * k.inv_d + a.eps) : 1.f;
     float gt = 1.f;
     if (k.gate == QLORA_GATE_TOKEN && live) gt = load_param<AT>(a.gate, k.wf32, row);
 
@@ -559,9 +567,9 @@ __global__ __launch_bounds__(WT) void k_resnorm_bwd_wide(qlora_resnorm_grad a, f
       }
     }
     row_sum<WT>(s3, slots3, slot3);
-    const float rsh = k.pre ? __builtin_amdgcn_rsqf(s3[0] * k.inv_d + a.eps) : 0.f;
+    const float rsh = k.pre ? inv_root(s3[0] * k.inv_d + a.eps) : 0.f;
     const float ch = s3[1] * rsh * k.inv_d;   // mean(A rms(h))
-    const float rsy = k.post ? __builtin_amdgcn_rsqf(s3[2] * k.inv_d + a.eps) : 1.f;
+    const float rsy = k.post ? inv_root(s3[2] * k.inv_d + a.eps) : 1.f;
     float gt = 1.f;
     if (k.gate == QLORA_GATE_TOKEN) gt = load_param<AT>(a.gate, k.wf32, row);
     auto upstream = [&](int c, float (&D)[EV]) {

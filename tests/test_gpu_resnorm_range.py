@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from oracle import train_ops as T
-from tests.test_gpu_resnorm import _case, _check, _close, _gate_np, _np, _rows
+from tests.test_gpu_resnorm import DT, _case, _check, _close, _gate_np, _np, _rows
 
 pytestmark = pytest.mark.gpu
 
@@ -50,22 +50,28 @@ def test_earlier_rows_beside_the_last(q, kind):
         assert dw[col].item() == want and torch.isfinite(dw).sum() == d - 1
 
 
-def _sized(q, g, m, d, act, res, kind, sh, sy, eps, offset=0.25):
+def _even(g, shape):
+    """Normal numbers, none smaller than a half in magnitude, so that no row is much smaller than 1."""
+    v = g.standard_normal(shape)
+    return np.sign(v) * np.maximum(np.abs(v), 0.5)
+
+
+def _sized(q, g, m, d, act, res, kind, sh, sy, eps, offset=0.25, extra=0.0):
     """Both directions with residual rows of the size `sh`, block outputs of the size `sy`, and gradients that keep both
     terms of dx of one size."""
     a = _case(g, m, d, act, res, "f32", kind, True, True)
-    a["x"], a["y"] = (_rows(g.standard_normal((m, d)) * s, t) for s, t in ((sh, res), (sy, act)))
+    a["x"], a["y"] = (_rows(_even(g, (m, d)) * s, t) for s, t in ((sh, res), (sy, act)))
     eps = float(np.float32(eps))
     kw = dict(scale=0.75, eps=eps, w_offset=offset)
     args = (_gate_np(a, kind), kind, _np(a["w_post"]), _np(a["w_pre"]), True, True, 0.75, eps, offset)
     h, z = q.qlora_resnorm_fwd(a["x"], a["y"], a["gate"], a["w_post"], a["w_pre"], **kw)
     hw, zw = T.resnorm_fwd(_np(a["x"]), _np(a["y"]), *args)
     mag = np.abs(_np(a["x"])) + np.abs(hw - _np(a["x"]))
-    _close(h, hw, mag, res, name="h")
+    _close(h, hw, mag, res, extra, name="h")
     r = 1 / np.sqrt((hw * hw).mean(1, keepdims=True) + eps)
     w = np.abs(offset + _np(a["w_pre"]))
-    _close(z, zw, r * w * (mag + np.abs(hw) * (r * r * (np.abs(hw) * mag).mean(1, keepdims=True))), act, name="z")
-    h, dz, dh = (_rows(g.standard_normal((m, d)) * s, t) for s, t in ((sh, res), (1.0, act), (1 / sh, res)))
+    _close(z, zw, r * w * (mag + np.abs(hw) * (r * r * (np.abs(hw) * mag).mean(1, keepdims=True))), act, extra, name="z")
+    h, dz, dh = (_rows(_even(g, (m, d)) * s, t) for s, t in ((sh, res), (1.0, act), (1 / sh, res)))
     for given in (None, dh):
         got = q.qlora_resnorm_bwd(dz, given, h, a["y"], a["gate"], a["w_post"], a["w_pre"], **kw)
         want, mg = T.resnorm_bwd(_np(dz), _np(given), _np(h), _np(a["y"]), *args)
@@ -74,7 +80,7 @@ def _sized(q, g, m, d, act, res, kind, sh, sy, eps, offset=0.25):
                 continue
             dt = res if k == "dx" else act if k == "dy" or (k == "dgate" and kind == "full") else "f32"
             col = k in ("dw_post", "dw_pre") or (k == "dgate" and kind == "channel")
-            _close(t if t.dim() == want[k].ndim else t[:, 0], want[k], mg[k], dt, m * 2.0 ** -24 if col else 0.0, k)
+            _close(t if t.dim() == want[k].ndim else t[:, 0], want[k], mg[k], dt, extra + (m * 2.0 ** -24 if col else 0.0), k)
 
 
 @pytest.mark.parametrize("size,eps", [(1e13, 1e-5), (1e15, 1e-5), (1e17, 1e-5), (1e-14, 0.0), (1e-14, 1e-30),
@@ -88,3 +94,27 @@ def test_large_and_small_rows(q, size, eps, d):
             _sized(q, g, 3, d, act, res, "channel", sh, sy, eps)
     for kind in ("none", "token", "full"):
         _sized(q, g, 3, d, "f32", "f32", kind, size, size, eps)
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-42])
+@pytest.mark.parametrize("d", [5, 64, 1001, 4096, 9000])
+def test_subnormal_mean_squares(q, eps, d):
+    """Rows of 2^-65, whose squares and their mean are subnormal.  Each square is off by half of the
+    spacing 2^-149 and so is the mean: 2^-149 in all, of a mean of 2^-130 and at least a quarter of that
+    in these rows, 2^-17 relative; its root is off by half of that, and the outputs hold at most three roots:
+    2^-14 covers them."""
+    g = np.random.default_rng(d)
+    size = 2.0 ** -65
+    for act, res in (("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")):
+        for sh, sy in ((size, 1.0), (1.0, size)):
+            _sized(q, g, 3, d, act, res, "channel", sh, sy, eps, extra=2.0 ** -14)
+        x, dz = _rows(_even(g, (3, d)) * size, res), _rows(g.standard_normal((3, d)), act)
+        w = torch.from_numpy(g.standard_normal(d).astype(np.float32)).cuda()
+        e = float(np.float32(eps))
+        _, z = q.qlora_resnorm_fwd(x, w_pre=w, eps=eps, act_dtype=DT[act])
+        _, zw = T.resnorm_fwd(_np(x), None, None, "none", None, _np(w), False, True, 1.0, e, 0.0)
+        _close(z, zw, np.abs(zw), act, 2.0 ** -14)
+        dx, _, _, _, dw = q.qlora_resnorm_bwd(dz, None, x, w_pre=w, eps=eps)
+        want, mg = T.resnorm_bwd(_np(dz), None, _np(x), None, None, "none", None, _np(w), False, True, 1.0, e, 0.0)
+        _close(dx, want["dx"], mg["dx"], res, 2.0 ** -14)
+        _close(dw, want["dw_pre"], mg["dw_pre"], "f32", 2.0 ** -14)
