@@ -197,7 +197,8 @@ struct Columns {
       }
     }
   }
-  // zeros in the place of the values left out
+  // zeros in the place of the values left out, and of their weights: an infinite
+  // weight of the thread before times zero would be no number
   template <int T>
   QL_DEV Raw<T, kVec> only_mine(int v, Raw<T, kVec> r) const {
     if constexpr (TAIL) {
@@ -211,6 +212,11 @@ struct Columns {
       }
     }
     return r;
+  }
+  QL_DEV void only_mine(int v, float (&w)[kVec]) const {
+    if constexpr (TAIL)
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) w[j] = j < skip[v] ? 0.f : w[j];
   }
   template <int T, bool STREAM>
   QL_DEV Raw<T, kVec> load(int v, const char* row) const {
@@ -247,6 +253,8 @@ __global__ __launch_bounds__(resnorm_fwd_block(G)) void k_resnorm_fwd(qlora_resn
     if (!at_col.in[v]) continue;
     if (k.branch) branch_weight<AT, EV>(wb[v], a, k, at_col.col[v], EV);
     if (k.pre) mul_weight<AT, true, EV>(wpre[v], a.w_pre, k.wf32, a.w_offset, at_col.col[v], EV);
+    at_col.only_mine(v, wb[v]);
+    at_col.only_mine(v, wpre[v]);
   }
 
   struct Row {
@@ -409,6 +417,8 @@ __global__ __launch_bounds__(kResnormBwdBlock) void k_resnorm_bwd(qlora_resnorm_
     if (!at_col.in[v]) continue;
     if (k.branch) branch_weight<AT, EV>(wb[v], a, k, at_col.col[v], EV);
     if (k.pre) mul_weight<AT, true, EV>(wpre[v], a.w_pre, k.wf32, a.w_offset, at_col.col[v], EV);
+    at_col.only_mine(v, wb[v]);
+    at_col.only_mine(v, wpre[v]);
   }
   using Row = GradRow<AT, RT, FULL>;
   auto load_row = [&](int64_t row, Row& r) {

@@ -118,3 +118,38 @@ def test_subnormal_mean_squares(q, eps, d):
         want, mg = T.resnorm_bwd(_np(dz), None, _np(x), None, None, "none", None, _np(w), False, True, 1.0, e, 0.0)
         _close(dx, want["dx"], mg["dx"], res, 2.0 ** -14)
         _close(dw, want["dw_pre"], mg["dw_pre"], "f32", 2.0 ** -14)
+
+
+def _alike(got, want):
+    """Finite, infinite (with its sign) and no number in the same places."""
+    got = _np(got)
+    return (np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(np.isinf(got), np.isinf(want))
+            and np.array_equal(np.sign(got[np.isinf(got)]), np.sign(want[np.isinf(want)])))
+
+
+@pytest.mark.filterwarnings("ignore::RuntimeWarning")
+@pytest.mark.parametrize("d", [5, 9, 64, 1001, 1500, 4097, 8191, 9001])
+def test_infinite_weight_near_the_end_of_a_row(q, d):
+    """An infinite weight acts on its own column and on what the formulas sum over, also where the row's last
+    vector lies over columns of the thread before."""
+    g = np.random.default_rng(d)
+    m = 3
+    for act, res in (("f32", "f32"), ("bf16", "f32"), ("f16", "f16")):
+        for col in sorted({max(0, d - 8), max(0, d // 8 * 8 - 1), d - 1}):
+            x, y, dz, dh = (_rows(_even(g, (m, d)), t) for t in (res, act, act, res))
+            w, bad = (torch.from_numpy(_even(g, d).astype(np.float32)).cuda() for _ in range(2))
+            bad[col] = float("inf")
+            for w_post, w_pre in ((bad, w), (w, bad)):
+                a = (None, "none", _np(w_post), _np(w_pre), True, True, 1.0, float(np.float32(1e-5)), 0.0)
+                h, z = q.qlora_resnorm_fwd(x, y, None, w_post, w_pre, eps=1e-5)
+                hw, zw = T.resnorm_fwd(_np(x), _np(y), *a)
+                assert _alike(h, hw) and _alike(z, zw)
+                # any residual for the backward: the ordinary x
+                got = q.qlora_resnorm_bwd(dz, dh, x, y, None, w_post, w_pre, eps=1e-5)
+                want, mg = T.resnorm_bwd(_np(dz), _np(dh), _np(x), _np(y), *a)
+                for k, t in zip(("dx", "dy", "dgate", "dw_post", "dw_pre"), got):
+                    assert t is None or _alike(t, want[k]), k
+                _close(got[4], want["dw_pre"], mg["dw_pre"], "f32", m * 2.0 ** -24)
+                if w_post is bad:
+                    _close(got[0], want["dx"], mg["dx"], res)
+                    _close(got[3], want["dw_post"], mg["dw_post"], "f32", m * 2.0 ** -24)
