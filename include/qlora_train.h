@@ -239,7 +239,8 @@ int qlora_grad_norm(const qlora_adamw *plan, float max_norm, float *out, void *w
  * The moments are read from `in` and written to `out` (the same buffers for a
  * step in place).  If c is not finite the step is skipped: p_out = p (and
  * copy = p rounded), out = in.  A gradient that is not finite otherwise
- * reaches p.
+ * reaches p.  With eps == 0 a second moment of 0 (a square below binary32's smallest number
+ * among them) is divided by, as the formula says.
  * 8-bit moments: p is updated from the fp32 moments of this step, which are
  * then rounded stochastically: a magnitude x goes to the grid with random
  * bits added below the kept mantissa bits, so that its expectation is x; a

@@ -167,12 +167,17 @@ __global__ __launch_bounds__(256) void k_adamw(const OptEntry* __restrict__ tab,
         v[j] = v[j] * k.b2 + (gj * gj) * k.c2;
       }
     }
+    if (k.small_eps) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float den = __builtin_amdgcn_sqrtf(v[j]) * k.rs_bc2 + k.eps;
-      // the update needs a relative accuracy far below its share of p: the
-      // one-ulp root and reciprocal are enough
-      pn[j] = p[j] * keep - rate * (m[j] * __builtin_amdgcn_rcpf(den));
+      for (int j = 0; j < 4; ++j) pn[j] = p[j] * keep - rate * (m[j] / (sqrtf(v[j]) * k.rs_bc2 + k.eps));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float den = __builtin_amdgcn_sqrtf(v[j]) * k.rs_bc2 + k.eps;
+        // the update needs a relative accuracy far below its share of p: the
+        // one-ulp root and reciprocal are enough
+        pn[j] = p[j] * keep - rate * (m[j] * __builtin_amdgcn_rcpf(den));
+      }
     }
     if constexpr (S8) {
       // (values past the tensor's end are zero in the state and have no gradient)

@@ -339,6 +339,7 @@ int qlora_adamw_step(const qlora_adamw* plan, const qlora_opt_state* in, const q
   k.lr_bc1 = (float)(h->lr / bc1);
   k.rs_bc2 = (float)(1 / std::sqrt(bc2));
   k.eps = (float)h->eps;
+  k.small_eps = k.eps < 0x1p-39f * k.rs_bc2;
   k.key = mix32(h->seed + 0x9E3779B9u * (uint32_t)h->step);
   const char* t = (const char*)plan->table;
   if (ql::launch_adamw((const ql::OptEntry*)(t + ql::kOptHead), (const ql::OptChunk*)(t + map_off(plan->count)), plan->chunks,

@@ -82,6 +82,11 @@ constexpr size_t kOptHead = 16;
 struct AdamwScalars {
   float b1, c1, b2, c2;    // beta, 1 - beta
   float lr, wd, lr_bc1, rs_bc2, eps;   // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
+  // The root and reciprocal instructions take subnormals for zero.  A subnormal v, whose root is
+  // below 2^-63, may count as zero where eps is 2^24 times what that root adds to the
+  // denominator; below that eps the update takes the full root and division (131M values with
+  // 8-bit moments 380 us, otherwise 353).
+  bool small_eps;
   uint32_t key;            // step key of the rounding bits
 };
 constexpr int kNormWgs = 256;   // most workgroups, and partial sums, of the gradient norm

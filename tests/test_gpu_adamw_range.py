@@ -1,0 +1,60 @@
+"""The AdamW step over the whole of its accepted range: eps of zero with subnormal second moments.
+Oracle and tolerances as in ``test_gpu_adamw.py``; a subnormal second moment
+is off by half the spacing 2^-149 at each of its three roundings besides."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import train_ops as T
+from tests.test_gpu_adamw import U, _np, _sections, _tensors
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def q():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import qlora_fine_tuning_nf4_amd as pkg
+    pkg.lib()
+    return pkg
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-42, 1e-30, 1e-20, 1e-12, 1e-8])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_subnormal_second_moments(q, bits, eps):
+    """Gradients near 1e-20: their squares are subnormal, the steps are as large as with any other."""
+    g = np.random.default_rng(bits)
+    sizes = [3000, 5]
+    b1, b2, lr, step = 0.9, 0.99, 0.01, 4
+    p, gr = _tensors(g, sizes, "f32"), _tensors(g, sizes, "f32")
+    for t in gr:
+        t.copy_(torch.from_numpy((np.sign(g.standard_normal(t.numel())) * g.uniform(1e-19, 3e-19, t.numel())).astype(np.float32)))
+    plan = q.qlora_adamw_init(p, gr, state_bits=bits)
+    st = plan.new_state()
+    if bits == 32:
+        for a, b in zip(_sections(st.m, sizes), _sections(st.v, sizes)):
+            a.copy_(torch.from_numpy((g.standard_normal(len(a)) * 1e-20).astype(np.float32)))
+            b.copy_(torch.from_numpy(g.uniform(1e-40, 1e-39, len(b)).astype(np.float32)))
+    m, v = (x.double().cpu().numpy() for x in st.moments())
+    p0 = [_np(t) for t in p]
+    q.qlora_adamw_step(plan, st, step, lr, betas=(b1, b2), eps=eps)
+    for i, x0 in enumerate(p0):
+        m0, v0 = _sections(m, sizes)[i], _sections(v, sizes)[i]
+        m1, v1 = T.adamw_moments(_np(gr[i]), m0, v0, b1, b2)
+        want = T.adamw_param(x0, m1, v1, step, lr, b1, b2, eps, 0.0)
+        size = lr / (1 - b1 ** step) * (b1 * np.abs(m0) + (1 - b1) * np.abs(_np(gr[i]))) / (
+            np.sqrt(v1 / (1 - b2 ** step)) + eps)
+        assert (np.abs(_np(p[i]) - want) <= (32 * U + 3 * 2.0 ** -150 / v1) * size + 4 * U * np.abs(x0)).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_subnormal_eps_beside_zero_moments(q, bits):
+    """Parameters that never had a gradient stay as they are for any eps above zero."""
+    g = np.random.default_rng(1)
+    p = _tensors(g, [700], "f32")
+    plan = q.qlora_adamw_init(p, [torch.zeros_like(p[0])], state_bits=bits)
+    before = p[0].clone()
+    for eps in (1e-44, 1e-40, 1e-20, 1e-8):
+        q.qlora_adamw_step(plan, plan.new_state(), 1, 0.1, eps=eps)
+        assert torch.equal(p[0], before)
