@@ -244,7 +244,10 @@ int qlora_grad_norm(const qlora_adamw *plan, float max_norm, float *out, void *w
  * 8-bit moments: p is updated from the fp32 moments of this step, which are
  * then rounded stochastically: a magnitude x goes to the grid with random
  * bits added below the kept mantissa bits, so that its expectation is x; a
- * positive second moment never becomes 0.  For value j of block b of the
+ * positive second moment never becomes 0.  A moment that is not finite (a
+ * gradient's infinity or NaN, or a square above binary32's range) is left out of its
+ * block's scale and gets the largest code with its sign, so that the block's other values
+ * are held as if it were 0.  For value j of block b of the
  * state, mod 2^32:
  *   mix(x): x ^= x >> 16; x *= 0x6A09E667; x ^= x >> 15; x *= 0xBB67AE85; x ^= x >> 16
  *   bits = mix(mix(mix(seed + 0x9E3779B9 step) + 0x510E527F b) + 0x9E3779B9 (j + 1))

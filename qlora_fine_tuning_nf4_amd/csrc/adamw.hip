@@ -77,7 +77,8 @@ QL_DEV uint32_t mix32(uint32_t x) {
 // emin), emin the grid's smallest normal exponent, which turns the grid's
 // subnormals into binary32's own, so that code = bits >> drop for both; the
 // random bits below the kept ones make the cut stochastic.  y <= top, which
-// is on the grid, so the carry never passes the largest code.
+// is on the grid, so the carry never passes the largest code.  An x that is not
+// finite gets the largest code (inf * inv is inf or NaN, and the minimum is top).
 QL_DEV uint32_t code8(float x, float inv, float top, float power, int drop, uint32_t rnd) {
   const float y = fminf(x * inv, top) * power;
   return (__builtin_bit_cast(uint32_t, y) + rnd) >> drop;
@@ -189,6 +190,18 @@ __global__ __launch_bounds__(256) void k_adamw(const OptEntry* __restrict__ tab,
       }
       am = wave_largest(am);
       av = wave_largest(av);
+      // (both uniform: compared as integers on the scalar unit)
+      if (max(__builtin_bit_cast(uint32_t, am), __builtin_bit_cast(uint32_t, av)) >= 0x7F800000u) {
+        // infinities stay out of the scales, as NaNs do: one value must not take its block along
+        float fm = 0.f, fv = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          fm = fmaxf(fm, fabsf(m[j]) < __builtin_inff() ? fabsf(m[j]) : 0.f);
+          fv = fmaxf(fv, v[j] < __builtin_inff() ? v[j] : 0.f);
+        }
+        am = wave_largest(fm);
+        av = wave_largest(fv);
+      }
       const bool some_m = am >= kTiny, some_v = av >= kTiny;
       // top / largest: the lower lanes divide for m, the upper ones for v
       const bool low = lane < 32;

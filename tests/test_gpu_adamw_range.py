@@ -58,3 +58,43 @@ def test_subnormal_eps_beside_zero_moments(q, bits):
     for eps in (1e-44, 1e-40, 1e-20, 1e-8):
         q.qlora_adamw_step(plan, plan.new_state(), 1, 0.1, eps=eps)
         assert torch.equal(p[0], before)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan"), 1e25])
+def test_one_bad_gradient_leaves_its_block(q, bad):
+    """8-bit moments: a value whose moments are not finite changes nothing of its block's other values, in
+    this step and the next, against a run where its gradient is 0."""
+    g = np.random.default_rng(9)
+    n, at = 600, 300
+    grads = [torch.from_numpy(g.standard_normal(n).astype(np.float32)).cuda() for _ in range(3)]
+    start = torch.from_numpy(g.standard_normal(n).astype(np.float32)).cuda()
+    runs = []
+    for value in (0.0, bad):
+        p, gr = start.clone(), grads[0].clone()
+        plan = q.qlora_adamw_init([p], [gr], state_bits=8)
+        st = plan.new_state()
+        steps = []
+        for t in range(3):
+            gr.copy_(grads[t])
+            if t < 2:
+                gr[at] = value if t else 0.0
+            q.qlora_adamw_step(plan, st, t + 1, 0.01, seed=5)
+            steps.append([x.clone() for x in (p, st.m.view(torch.uint8), st.v.view(torch.uint8), st.m_scale, st.v_scale)])
+        runs.append(steps)
+    other = torch.arange(n, device="cuda") != at
+    code = (torch.arange(768, device="cuda") != at).view(3, 256)
+    good, got = (r[1] for r in runs)
+    assert torch.equal(got[2][code], good[2][code]) and torch.equal(got[4], good[4])
+    assert got[2].view(-1)[at] == 0x7B                                 # 57344 in e5m2
+    if abs(bad) != 1e25:                                               # 1e25: a finite first moment, and the block's largest
+        assert torch.equal(got[1][code], good[1][code]) and torch.equal(got[3], good[3])
+        assert got[1].view(-1)[at] & 0x7F == 0x7E                      # 448 in e4m3
+        if bad == bad:
+            assert (got[1].view(-1)[at] >= 0x80) == (bad < 0)
+    good, got = (r[2] for r in runs)
+    assert torch.isfinite(got[0][other]).all()
+    if abs(bad) != 1e25:
+        assert torch.equal(got[0][other], good[0][other])
+        assert torch.isnan(got[0][at])
+        # the third step's own gradient at the place is an ordinary one: the scales may hold it
+        assert torch.isfinite(got[3]).all() and torch.isfinite(got[4]).all()
