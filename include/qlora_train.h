@@ -7,8 +7,10 @@
  * Conventions are those of qlora_nf4.h: device pointers owned by the caller,
  * nothing allocated, freed or synchronized (qlora_adamw_init excepted), work
  * enqueued on `stream`, every argument checked before the first HIP call,
- * positive QLORA_ERR_* statuses (qlora_strerror), no state kept between
- * calls, deterministic results (the same inputs give the same bits).
+ * positive QLORA_ERR_* statuses (qlora_strerror), deterministic results (the
+ * same inputs give the same bits).  Nothing that a result depends on is kept between calls;
+ * qlora_grad_norm alone writes to memory of the plan while it runs, so that two of
+ * its calls on one plan must not overlap.
  * Dtypes are QLORA_F32, QLORA_BF16 and QLORA_F16.  Matrices are row-major
  * with unit column stride; ld* is the row stride in elements (>= the row
  * width).  Tensors need the alignment of one element only; rows that start on
@@ -225,7 +227,9 @@ size_t qlora_grad_norm_workspace_bytes(const qlora_adamw *plan);
  * that brings it to max_norm: min(1, max_norm / (out[0] + 1e-6)), 1 when max_norm <= 0,
  * NaN when out[0] is not finite (a step given that factor is
  * skipped).  out: 2 floats on the device.  The call counts its workgroups in the plan's
- * table: two calls on one plan must not overlap.
+ * table, zero again when it ends: two calls on one plan must not overlap, whatever
+ * streams, workspaces and outputs they have (their results would be undefined; later
+ * calls are not affected).  The step only reads the table.
  */
 int qlora_grad_norm(const qlora_adamw *plan, float max_norm, float *out, void *workspace,
                     size_t workspace_bytes, void *stream);

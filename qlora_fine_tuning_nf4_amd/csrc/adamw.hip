@@ -244,8 +244,10 @@ __global__ __launch_bounds__(256) void k_adamw(const OptEntry* __restrict__ tab,
 
 // Norm of all gradients and its clip factor.  Every workgroup leaves the sum of
 // squares of its chunks; the one that arrives last, by a count kept in the
-// plan's table, adds the sums in the order of their index and sets the count
-// back to zero.  No workgroup waits for another.  The sums cross XCDs, whose
+// plan's table, adds the sums in the order of their index.  The count wraps to zero
+// with the last arrival: a call finds it at zero whatever came before, also after
+// calls that overlapped (whose own results are then undefined).  No workgroup
+// waits for another.  The sums cross XCDs, whose
 // L2s are not coherent: they are written and read with device-scope atomics,
 // which act at the level the XCDs share, and the count is raised only after
 // the write is done (the wait on the vector-memory counter).  A release fence
@@ -316,7 +318,7 @@ __global__ __launch_bounds__(kNormThreads) void k_grad_norm(const OptEntry* __re
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     QL_VMCNT(0);
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    last = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+    last = atomicInc(arrived, gridDim.x - 1) == gridDim.x - 1;
   }
   __syncthreads();
   if (!last) return;
@@ -328,7 +330,6 @@ __global__ __launch_bounds__(kNormThreads) void k_grad_norm(const OptEntry* __re
     if (!(norm < __builtin_inff())) f = __builtin_nanf("");
     out[0] = norm;
     out[1] = f;
-    __hip_atomic_store(arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
 }
 

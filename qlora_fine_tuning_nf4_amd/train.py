@@ -451,7 +451,8 @@ def qlora_grad_norm_workspace_bytes(plan: AdamWPlan) -> int:
 
 def qlora_grad_norm(plan: AdamWPlan, max_norm: float = 0.0, out=None, workspace=None) -> torch.Tensor:
     """-> float32 [2] on the device: the norm of all gradients, and the factor that brings it to
-    max_norm (pass out[1:] to qlora_adamw_step as grad_scale)."""
+    max_norm (pass out[1:] to qlora_adamw_step as grad_scale).  Calls on one plan must not overlap on
+    the device: on different streams, let one wait for the other."""
     if out is None:
         out = torch.empty(2, dtype=torch.float32, device=plan.device)
     if workspace is None:

@@ -98,3 +98,20 @@ def test_one_bad_gradient_leaves_its_block(q, bad):
         assert torch.isnan(got[0][at])
         # the third step's own gradient at the place is an ordinary one: the scales may hold it
         assert torch.isfinite(got[3]).all() and torch.isfinite(got[4]).all()
+
+
+def test_norm_after_calls_that_overlapped(q):
+    """Two calls on one plan at a time are against the rule and may return anything, but the next call is right."""
+    p = torch.zeros(1 << 28, device="cuda")      # long enough for the calls to run side by side
+    gr = torch.ones_like(p)
+    plan = q.qlora_adamw_init([p], [gr])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for s in streams:
+            with torch.cuda.stream(s):
+                q.qlora_grad_norm(plan, 1.0)
+    torch.cuda.synchronize()
+    for value in (1.0, 0.5):
+        gr.fill_(value)
+        assert q.qlora_grad_norm(plan)[0].item() == 16384 * value
+    assert not plan.table[:4].any()
