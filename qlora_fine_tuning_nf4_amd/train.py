@@ -290,7 +290,8 @@ def qlora_resnorm_bwd(dz, dh, h: torch.Tensor, y=None, gate=None, w_post=None, w
                       w_offset: float = 0.0, outs=None, need=(True, True, True, True),
                       workspace=None):
     """-> (dx, dy, dgate, dw_post, dw_pre), None where there is nothing to compute.  `need` switches
-    (dy, dgate, dw_post, dw_pre) off; `outs` gives the five output tensors."""
+    (dy, dgate, dw_post, dw_pre) off; `outs` gives the five output tensors (None: not computed; one for
+    something that the call does not compute is left as it is, and None is returned in its place)."""
     ref = h if h is not None else dh
     shape, res, dev = ref.shape, ref.dtype, ref.device
     m, d = shape
@@ -317,6 +318,14 @@ def qlora_resnorm_bwd(dz, dh, h: torch.Tensor, y=None, gate=None, w_post=None, w
                 e((d,), f32) if post and need[2] else None,
                 e((d,), f32) if pre and need[3] else None)
     dx, dy, dgate, dw_post, dw_pre = outs
+    if y is None:
+        dy = None
+    if not kind:
+        dgate = None
+    if not post:
+        dw_post = None
+    if not pre:
+        dw_pre = None
     # rows: pointer and stride
     rows = []
     for t, dt, name in ((dz, act, "dz"), (dh, res, "dh"), (h, res, "h"), (y, act, "y"), (dx, res, "dx"), (dy, act, "dy"),
