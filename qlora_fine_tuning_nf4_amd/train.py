@@ -94,16 +94,14 @@ def _check(status, what):
         _b._check(status, what)
 
 
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-
-
 def _stream(device):
     """The current HIP stream of the tensors' device, which must be the current device.  The raw
-    handle is asked for: building a torch.cuda.Stream object takes 2.8 us, as much as a launch."""
+    handle is asked for: building a torch.cuda.Stream object takes 2.8 us, as much as a launch.  A torch
+    without GPU support lacks these names, but has no tensor that gets to them."""
     i = device.index
-    if i is None or i != _current_device():
+    if i is None or i != torch._C._cuda_getDevice():
         raise QLoRAError(f"tensors must be on the current GPU, not on {device}")
-    return _raw_stream(i)
+    return torch._C._cuda_getCurrentRawStream(i)
 
 
 def _dt(t, name):
