@@ -60,22 +60,16 @@ QL_DEV void store1(void* p, int64_t i, float v) {
 template <int T, int N, bool STREAM = false>
 QL_DEV Raw<T, N> loadv(const void* p, int i, int left) {
   constexpr int W = N * kElBytes<T> / 4;
+  static_assert(W % 4 == 0);
   Raw<T, N> r;
   if (left >= N) {
     const char* at = reinterpret_cast<const char*>(p) + (uint32_t)(i * kElBytes<T>);
-    if constexpr (W == 2) {
-      const QL_GLOBAL u32x2_a2_t* q = (const QL_GLOBAL u32x2_a2_t*)at;
-      const u32x2_t v = STREAM ? __builtin_nontemporal_load(q) : *q;
-      r.w[0] = v[0];
-      r.w[1] = v[1];
-    } else {
 #pragma unroll
-      for (int h = 0; h < W / 4; ++h) {
-        const QL_GLOBAL u32x4_a2_t* q = (const QL_GLOBAL u32x4_a2_t*)(at + 16 * h);
-        const u32x4_t v = STREAM && W == 4 ? __builtin_nontemporal_load(q) : *q;
+    for (int h = 0; h < W / 4; ++h) {
+      const QL_GLOBAL u32x4_a2_t* q = (const QL_GLOBAL u32x4_a2_t*)(at + 16 * h);
+      const u32x4_t v = STREAM && W == 4 ? __builtin_nontemporal_load(q) : *q;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) r.w[4 * h + j] = v[j];
-      }
+      for (int j = 0; j < 4; ++j) r.w[4 * h + j] = v[j];
     }
   } else if constexpr (T == kElF32) {
     // the row's last element stands in for those past it: all loads are in
@@ -110,25 +104,19 @@ QL_DEV float el(const Raw<T, N>& r, int j) {
 template <int T, int N, bool STREAM = false>
 QL_DEV void storev(void* p, int i, int left, const float (&f)[N]) {
   constexpr int W = N * kElBytes<T> / 4;
+  static_assert(W % 4 == 0);
   if (left >= N) {
     uint32_t w[W];
 #pragma unroll
     for (int j = 0; j < W; ++j)
       w[j] = T == kElF32 ? __builtin_bit_cast(uint32_t, f[j]) : pack16x2<T == kElF16>(f[2 * j % N], f[(2 * j + 1) % N]);
     char* at = reinterpret_cast<char*>(p) + (uint32_t)(i * kElBytes<T>);
-    if constexpr (W == 2) {
-      QL_GLOBAL u32x2_a2_t* q = (QL_GLOBAL u32x2_a2_t*)at;
-      const u32x2_t v = {w[0], w[1]};
-      if (STREAM) __builtin_nontemporal_store((u32x2_a2_t)v, q);
-      else *q = v;
-    } else {
 #pragma unroll
-      for (int h = 0; h < W / 4; ++h) {
-        QL_GLOBAL u32x4_a2_t* q = (QL_GLOBAL u32x4_a2_t*)(at + 16 * h);
-        const u32x4_t v = {w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]};
-        if (STREAM && W == 4) __builtin_nontemporal_store((u32x4_a2_t)v, q);
-        else *q = v;
-      }
+    for (int h = 0; h < W / 4; ++h) {
+      QL_GLOBAL u32x4_a2_t* q = (QL_GLOBAL u32x4_a2_t*)(at + 16 * h);
+      const u32x4_t v = {w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]};
+      if (STREAM && W == 4) __builtin_nontemporal_store((u32x4_a2_t)v, q);
+      else *q = v;
     }
     return;
   }

@@ -13,7 +13,6 @@ from . import binding as _b
 from .binding import QLoRAError
 
 _DT = _b._DTYPE_ENUM
-GATES = {"none": 0, "channel": 1, "token": 2, "full": 3}
 ADAMW_BLOCK = 256
 _c = ctypes
 _vp, _i64, _i32, _f32, _f64, _sz = (_c.c_void_p, _c.c_int64, _c.c_int32, _c.c_float, _c.c_double,
