@@ -412,11 +412,14 @@ def qlora_adamw_init(params, grads, copies=None, params_out=None, state_bits: in
                      wd_mul=None) -> AdamWPlan:
     """Plan of one step over lists of tensors: params read, params_out (default: params) written,
     copies (optional, bf16 or fp16) written too.  lr_mul, wd_mul: a number a tensor.  Setup time:
-    writes the device table and synchronizes."""
+    writes the device table and synchronizes.  The plan holds the tensors and steps on their memory:
+    write new gradients into the tensors given here (no new ones in their place), or make another plan."""
     n = len(params)
     outs = params_out if params_out is not None else params
     if not n or len(grads) != n or len(outs) != n or (copies is not None and len(copies) != n):
         raise QLoRAError("params, grads, params_out and copies must be lists of one length, at least 1")
+    if any(k is not None and len(k) != n for k in (lr_mul, wd_mul)):
+        raise QLoRAError("lr_mul and wd_mul must have a number for every tensor")
     dev = params[0].device
     for name, ts in (("params", params), ("grads", grads), ("params_out", outs), ("copies", copies or [])):
         for t, p in zip(ts, params):
@@ -477,7 +480,7 @@ def qlora_adamw_step(plan: AdamWPlan, state: AdamWState, step: int, lr: float, b
                      state_out=None) -> None:
     """One step (step counts from 1) over the plan's tensors; moments from `state` to `state_out`
     (default: in place).  grad_scale: a one-element float32 device tensor multiplying the gradients; a value
-    that is not finite skips the step."""
+    that is not finite skips the step.  A captured step repeats its step count and settings on every replay."""
     s = plan._state(state)
     o = s if state_out is None or state_out is state else plan._state(state_out)
     gs = None

@@ -36,3 +36,13 @@ def test_outputs_that_a_call_does_not_compute(q, d):
                 assert got[i] is given[i] and torch.equal(got[i], want[i])
             else:
                 assert got[i] is None and want[i] is None and (given[i] == 7).all()
+
+
+@pytest.mark.parametrize("name", ["lr_mul", "wd_mul"])
+def test_multipliers_of_another_length(q, name):
+    p = [torch.ones(5, device="cuda"), torch.ones(3, device="cuda")]
+    g = [t.clone() for t in p]
+    for k in ([1.0], [], [1.0, 1.0, 1.0]):
+        with pytest.raises(q.QLoRAError, match="for every tensor"):
+            q.qlora_adamw_init(p, g, **{name: k})
+    assert q.qlora_adamw_init(p, g, **{name: [1.0, 0.5]}).blocks == 2
