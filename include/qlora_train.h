@@ -15,7 +15,10 @@
  * with unit column stride; ld* is the row stride in elements (>= the row
  * width).  Tensors need the alignment of one element only; rows that start on
  * 16 bytes are read and written fastest.  Sums, means and optimizer moments
- * are formed in binary32; every output is rounded once, to nearest even.
+ * are formed in binary32; every output is rounded once, to nearest even.  Inside,
+ * the norms' reciprocal roots and the root and reciprocal of the AdamW update are those of
+ * the instructions, good to one unit in the last place of binary32 (the update's are
+ * rounded to nearest where eps is below 2^-39 / sqrt(1 - beta2^t)).
  */
 #ifndef QLORA_TRAIN_H
 #define QLORA_TRAIN_H
@@ -209,8 +212,9 @@ size_t qlora_adamw_table_bytes(const int64_t *n, int count);
  * aligned, >= qlora_adamw_table_bytes) with a blocking copy: this call
  * synchronizes, but only with that copy: earlier work on the table's memory must have
  * ended.  All tensors share p_dtype, g_dtype (any dtype each) and, where copies are
- * given, copy_dtype (QLORA_BF16 or QLORA_F16, with p_dtype QLORA_F32).  The buffers named must stay
- * valid while the plan is used.  n == 0 tensors are allowed.
+ * given, copy_dtype (QLORA_BF16 or QLORA_F16, with p_dtype QLORA_F32).  The plan holds the
+ * buffers' addresses: they must stay valid while it is used, each step reads its gradients from
+ * them, and gradients at other addresses need another plan.  n == 0 tensors are allowed.
  * QLORA_ERR_NULL; QLORA_ERR_SHAPE: n < 0, or 2^31 blocks or more in all;
  * QLORA_ERR_ARG: count outside [1, QLORA_ADAMW_MAX_TENSORS], state_bits not 8
  * or 32, a non-finite multiplier; QLORA_ERR_DTYPE; QLORA_ERR_ALIGN; QLORA_ERR_WORKSPACE: table_bytes too
@@ -256,6 +260,9 @@ int qlora_grad_norm(const qlora_adamw *plan, float max_norm, float *out, void *w
  *   mix(x): x ^= x >> 16; x *= 0x6A09E667; x ^= x >> 15; x *= 0xBB67AE85; x ^= x >> 16
  *   bits = mix(mix(mix(seed + 0x9E3779B9 step) + 0x510E527F b) + 0x9E3779B9 (j + 1))
  * m takes the low and v the high 16 bits.
+ * The settings in `h` are read when the call is made: a captured step repeats them, its
+ * step count among them, on every replay.  Only *grad_scale, the gradients, the parameters and
+ * the state are read on the device.
  * QLORA_ERR_ARG: step < 1, beta1 or beta2 outside [0, 1), lr, eps or weight_decay negative
  * or not finite, a handle not filled by qlora_adamw_init.
  */
