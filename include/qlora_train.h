@@ -92,7 +92,9 @@ enum {
  *   p = post ? rms(y) * (w_offset + w_post) : y
  *   h = x + scale * gate * p                                  (new residual)
  *   z = rms(h) * (w_offset + w_pre)      when pre             (next block's input)
- * z uses h before its rounding to res_dtype.  With y == NULL there is no
+ * z uses h before its rounding to res_dtype.  A row's squares are summed in binary32: one
+ * whose sum passes its range counts as infinitely large (rms(u) = 0), and with eps == 0 a
+ * row of zeros divides by zero (NaN).  With y == NULL there is no
  * branch: z = rms(x) * (w_offset + w_pre); post, gate_kind, h are then ignored and
  * pre must be set.  A NULL w_post / w_pre stands for w_offset + w = 1.
  * x, h in res_dtype (QLORA_F32 or act_dtype); y, z and a full gate in

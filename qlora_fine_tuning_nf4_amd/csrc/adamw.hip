@@ -1,10 +1,10 @@
 // AdamW over all tensors of a plan in one launch, and the global gradient
 // norm.  Both are streams over memory: 28 bytes a value with fp32 moments and
 // fp32 gradients, 16 with 8-bit moments (2 more with a 16-bit copy).
-// Measured: 8.4M values of 256 tensors, fp32 moments and bf16 copies 44 us (5.7
-// TB/s; 51 with the norm and its clip factor before it), 56M of 280 tensors with 8-bit
-// moments 165 us (6.2 TB/s), one tensor of 131M with bf16 gradients 350 us
-// (6.0 TB/s).
+// Measured: 8.4M values of 256 tensors, fp32 moments and bf16 copies 41 us (6.1
+// TB/s; 52 with the norm and its clip factor before it), 56M of 280 tensors with 8-bit
+// moments 164 us (6.2 TB/s), one tensor of 131M with bf16 gradients 347 us
+// (6.1 TB/s).
 //
 // The plan's tensors are cut into chunks of 1024 consecutive values, each
 // within one tensor; a workgroup looks its chunk up in the plan's map (one

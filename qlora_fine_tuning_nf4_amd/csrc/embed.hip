@@ -20,9 +20,9 @@
 // Measured: lookup of 20001 rows of 8192 fp32 values to bf16 103 us (5.1 TB/s
 // with every table row counted once; repeats come from the caches), 16 rows
 // 4 us on the device.  Gradient of 32768 tokens of 4096 into a bf16 table of
-// 32000 rows 148 us: sort 28, sum and zero rows 112 (4.9 TB/s), join 9; of
-// 2048 tokens into an fp32 table 113 us: sort 7, sum and zero rows 97 (5.6
-// TB/s, nearly all of it zero rows), join 9.  The sort is bound by the latency of
+// 32000 rows 147 us: sort 28, sum and zero rows 111 (4.8 TB/s), join 9; of
+// 2048 tokens into an fp32 table 113 us: sort 7, sum and zero rows 100 (5.4
+// TB/s, nearly all of it zero rows), join 7.  The sort is bound by the latency of
 // cold ids and of its own code, the join by four dependent loads.
 #include <algorithm>
 

@@ -25,9 +25,9 @@
 // 1e15, or of 1e-14 with eps = 0).
 //
 // Measured: forward of 4096 x 8192 (bf16, fp32 residual) 76 us, 5.3 TB/s;
-// 16384 x 4096 (bf16) 94 us, 5.7 TB/s; one row 3.3 us on the device.  Backward
-// of 16384 x 4096 with all gradients 151 us, 5.3 TB/s (HBM traffic equal to the
-// operands; 500 vector instructions a row and wave, a third of the issue
+// 16384 x 4096 (bf16) 95 us, 5.7 TB/s; one row 3.3 us on the device.  Backward
+// of 16384 x 4096 with all gradients 154 us, 5.2 TB/s (HBM traffic equal to the
+// operands; 520 vector instructions a row and wave, a third of the issue
 // slots).  Bound by memory in large calls; in small ones by the dependent
 // steps of a row (load, two sums, store: 3 to 4 us) and the launches.
 #include <type_traits>
@@ -320,7 +320,7 @@ __global__ __launch_bounds__(resnorm_fwd_block(G)) void k_resnorm_fwd(qlora_resn
 }
 
 // Threads to a row that the register kernels do not hold: 1024 where it is
-// wide (4096 x 16384 bf16 forward 158 us; backward with column sums 333 us),
+// wide (4096 x 16384 bf16 forward 157 us; backward with column sums 328 us),
 // one wave where it is narrower than a vector (16384 x 5 forward 22 us, with
 // 1024 threads 217).
 constexpr int kWideThreads = 1024, kNarrowThreads = 64;

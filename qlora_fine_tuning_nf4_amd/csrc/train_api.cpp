@@ -111,7 +111,7 @@ ResnormBwdPlan resnorm_bwd_plan(int64_t m, int64_t d) {
   ResnormBwdPlan p;
   const bool wide = resnorm_wide(d);
   const int64_t side = wide ? 1 : kResnormBwdBlock / resnorm_threads(d);   // rows a workgroup holds at a time
-  // wide rows: 4096 x 16384 333 us with 128, 370 with 256 (more column sums to join); rows under a
+  // wide rows: 4096 x 16384 328 us with 128, 370 with 256 (more column sums to join); rows under a
   // vector: 16384 x 5 96 us with 1024, 136 with 256 (one thread walks a part's rows)
   const int64_t most = d < 8 ? 1024 : wide ? 128 : 256;
   p.wgs = (int)std::max<int64_t>(1, std::min<int64_t>(cdiv(m, side), most));
